@@ -1,0 +1,37 @@
+"""The 8-bit operators on the GPU at their limits: moments near the smallest numbers, steps of more than one launch,
+products whose sums are split, the 8-bit instruction's own error, and arrays past 2^31 values."""
+import numpy as np
+import pytest
+import torch
+
+import qlora_fine_tuning_quantize_amd as q
+from tests import ref8
+from tests.helpers import f64, host
+from tests.test_gpu_8bit import DEV, DTYPES, Many, assert_product, bits8, matrix
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- AdamW over many tensors ----
+
+@pytest.mark.parametrize("grad,eps", [("fp32", 1e-8), ("fp32", 1e-15), ("fp32", 1e-30), ("bf16", 1e-30)])
+def test_adamw_many_small_second_moments(grad, eps):
+    """Gradients whose squares are subnormal in fp32, or vanish, under an eps that does not hide them: parameters stay
+    within 2^-21 of their step, which the root of a second moment taken for 0 would make up to 1e10 times as large."""
+    print(f"adamw_many small second moments {grad} eps={eps}", flush=True)
+    t = Many([5000, 257, 1024, 3], grad, "bf16", 8, 31)
+    gen = torch.Generator().manual_seed(32)
+    for i, n in enumerate(t.sizes):
+        # 1e-13 .. 1e-24: of (1 - beta2) g^2 the normal, the subnormal and what is below the smallest number
+        size = 10.0 ** -(13 + 11 * torch.rand(n, generator=gen, dtype=torch.float64))
+        t.g[i] = (size * (1 - 2 * torch.randint(0, 2, (n,), generator=gen))).to(DTYPES[grad])
+        t.dg[i].copy_(t.g[i])
+        for codes, scale in (t.m[i], t.v[i]):
+            codes[:], scale[:] = 0, 0
+        for x in (t.dm[i].view(torch.uint8), t.dv[i].view(torch.uint8), t.dms[i], t.dvs[i]):
+            x.zero_()
+    for step in (1, 2, 3):
+        q.adamw_step_many(t.plan, lr=1e-3, step=step, eps=eps, seed=5)
+        t.step(step, None, 5, lr=1e-3, eps=eps)
+        torch.cuda.synchronize()
+        t.check(f"step {step}")

@@ -147,10 +147,14 @@ typedef struct ql_adamw_tensor {
  * One AdamW step over `count` tensors, in place, up to 960 in one launch: for
  * each the update of ql_adamw_step, bit for bit with 32-bit moments and no
  * grad_scale.
- *   t           host array of count structs; no two may share memory
- *   t_device    the same array in device memory, 16-byte aligned (uploaded
- *               once, it serves every step), left unchanged until the step is
- *               done: n is read from t, pointers from here
+ *   t           host array of count structs; no two may share memory.  It is
+ *               what is checked, and its n make the grid
+ *   t_device    the same array in device memory, byte for byte, n included,
+ *               16-byte aligned (uploaded once, it serves every step), left
+ *               unchanged until the step is done.  The kernel reads a tensor's
+ *               pointers and its n from here; a struct that differs from t's is
+ *               not found out, and its tensor is updated in part, or written
+ *               past its end
  *   grad_dtype  QL_F32, QL_BF16 or QL_F16
  *   state_bits  32 or 8
  *   copy_dtype  QL_BF16 or QL_F16 (ignored where no tensor has a copy)

@@ -45,7 +45,8 @@ size_t fp8_matmul_partial_floats(int64_t M, int64_t N, int64_t K);
 int launch_fp8_matmul(const ql_fp8 *a, const ql_fp8 *b, void *out, int out_dtype, bool accumulate,
                       float *part, hipStream_t stream);
 
-// adam_many.hip: t holds count checked tensors, table the same in device memory
+// adam_many.hip: t holds count checked tensors, table the same in device memory,
+// byte for byte (the kernel takes n from there)
 constexpr int kAdamTable = 960;               // tensors per launch (4 bytes of arguments each)
 constexpr int64_t kAdamMaxN = 1ll << 33;      // values of one tensor
 int launch_adamw_many(int32_t count, const ql_adamw_tensor *t, const ql_adamw_tensor *table,

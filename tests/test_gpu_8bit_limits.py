@@ -35,3 +35,12 @@ def test_adamw_many_small_second_moments(grad, eps):
         t.step(step, None, 5, lr=1e-3, eps=eps)
         torch.cuda.synchronize()
         t.check(f"step {step}")
+
+
+def test_adamw_table_is_the_structs():
+    """The kernel reads the structs, each tensor's n among them, from device memory: they are the host's, byte for byte."""
+    t = Many([5, 0, 300, 1025], "bf16", "fp16", 8, 41)
+    assert t.plan._table.dtype == t.plan._structs.dtype and t.plan._table.is_contiguous()
+    assert torch.equal(t.plan._table.cpu(), t.plan._structs)
+    assert t.plan._structs[:, 7].tolist() == t.sizes
+    assert t.plan._structs[:, 0].tolist() == [x.data_ptr() for x in t.dp]

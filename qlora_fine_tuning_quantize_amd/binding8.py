@@ -241,8 +241,9 @@ class AdamWTensors:
                  list(exp_avg_sq_scales) if eight else none,
                  list(copies) if copies is not None else none]
         _need(all(len(x) == n for x in lists), "the lists are of one length")
-        grad_type = grads[0].dtype if n else torch.float32
-        copy_type = next((c.dtype for c in lists[6] if c is not None), torch.bfloat16)
+        tensors = lambda given: (t for t in given if isinstance(t, torch.Tensor))
+        grad_type = next((g.dtype for g in tensors(lists[1])), torch.float32)
+        copy_type = next((c.dtype for c in tensors(lists[6])), torch.bfloat16)
         _need(copy_type in (torch.bfloat16, torch.float16), f"copies are {copy_type}: bf16 or fp16")
         types = (torch.float32, grad_type, torch.float8_e4m3fn if eight else torch.float32,
                  torch.float8_e5m2 if eight else torch.float32, torch.float32, torch.float32,
@@ -250,9 +251,9 @@ class AdamWTensors:
         names = ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale",
                  "copy")
         self._tensors = lists
-        dev = params[0].device if n else None
-        index = params[0].get_device() if n else None
-        sizes = [p.numel() for p in lists[0]]
+        first = next(tensors(lists[0]), None)
+        dev, index = (None, None) if first is None else (first.device, first.get_device())
+        sizes = [p.numel() if isinstance(p, torch.Tensor) else 0 for p in lists[0]]
         blocks = [-(-m // STATE_BLOCK) for m in sizes]
         spans, columns = [], []
         for k, (name, dtype, given) in enumerate(zip(names, types, lists)):
@@ -263,8 +264,8 @@ class AdamWTensors:
             for i, (t, m) in enumerate(zip(given, wanted)):
                 if t is None and k == 6:
                     continue
-                if not (t is not None and t.dtype == dtype and t.numel() == m and t.is_contiguous()
-                        and t.get_device() == index >= 0):
+                if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.numel() == m
+                        and t.is_contiguous() and t.get_device() == index >= 0):
                     raise ValueError(f"{name} {i}: a contiguous {dtype} tensor of {m} values on "
                                      f"{dev}, the parameters' GPU")
             at = [0 if t is None else t.data_ptr() for t in given]
@@ -300,6 +301,7 @@ class AdamWTensors:
         """With moments of zeros, in 8 or 32 bits, made here (exp_avgs,
         exp_avg_sqs and their scales are attributes)."""
         _need(bits in (8, 32), f"bits is {bits}: 8 or 32")
+        _need(all(isinstance(p, torch.Tensor) for p in params), "params are tensors")
         mk = lambda p, dt: torch.zeros(p.numel(), dtype=torch.uint8 if bits == 8 else torch.float32,
                                        device=p.device).view(dt)
         sc = lambda p: torch.zeros(-(-p.numel() // STATE_BLOCK), device=p.device)

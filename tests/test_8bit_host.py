@@ -216,6 +216,27 @@ def test_binding_refuses_what_is_not_on_the_gpu():
         q.AdamWTensors.zeros([x], [x.clone()], bits=4)
 
 
+@pytest.mark.parametrize("which", ["params", "grads", "exp_avgs", "exp_avg_sqs", "exp_avg_scales", "copies"])
+@pytest.mark.parametrize("bad", [None, 3.0])
+def test_binding_refuses_what_is_no_tensor(which, bad, monkeypatch):
+    """As a gradient that the backward has not made yet: first in its list, or later."""
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)  # checks alone: nothing is launched
+    for at in (0, 1):
+        dtype = {"exp_avgs": torch.float8_e4m3fn, "exp_avg_sqs": torch.float8_e5m2}
+        lists = {n: [torch.zeros(4, dtype=torch.uint8).view(dtype[n]) if n in dtype else torch.zeros(4) for _ in range(2)]
+                 for n in ("params", "grads", "exp_avgs", "exp_avg_sqs")}
+        lists |= {n: [torch.zeros(1) for _ in range(2)] for n in ("exp_avg_scales", "exp_avg_sq_scales")}
+        lists["copies"] = [torch.zeros(4, dtype=torch.float16) for _ in range(2)]
+        lists[which][at] = bad
+        if which == "copies" and bad is None:
+            lists["copies"][at], lists["exp_avg_sq_scales"][at] = None, None  # a tensor may have no copy, but needs scales
+        with pytest.raises(ValueError, match=f" {at}: a contiguous"):
+            q.AdamWTensors(**lists)
+        if which == "params":
+            with pytest.raises(ValueError):
+                q.AdamWTensors.zeros(lists["params"], lists["grads"])
+
+
 def test_shared_memory_is_found():
     """Written memory must not be given twice, nor be read elsewhere; gradients may be shared."""
     check = q.AdamWTensors._no_overlap

@@ -44,3 +44,36 @@ def test_adamw_table_is_the_structs():
     assert torch.equal(t.plan._table.cpu(), t.plan._structs)
     assert t.plan._structs[:, 7].tolist() == t.sizes
     assert t.plan._structs[:, 0].tolist() == [x.data_ptr() for x in t.dp]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("count", [960, 961, 2000])
+def test_adamw_many_launches(bits, count):
+    """As many tensors as a launch takes (960), one more, and three launches' worth, some of them empty, at a launch's
+    borders too: every tensor is updated once, and 8-bit moments are rounded by the tensor's place among all."""
+    print(f"adamw_many launches bits={bits} count={count}", flush=True)
+    sizes = [(37 * i) % 611 if i % 5 else 0 for i in range(count)]
+    for i, n in ((0, 0), (1, 1300), (63, 2000), (64, 3), (958, 700), (959, 0), (960, 0), (961, 1025), (1918, 5),
+                 (1919, 1), (1920, 513)):
+        if i < count:
+            sizes[i] = n
+    sizes[-1] = 300
+    t = Many(sizes, "bf16", "bf16", bits, 51)
+    for step in (1, 2):
+        q.adamw_step_many(t.plan, lr=2e-3, step=step, seed=77)
+        t.step(step, None, 77, lr=2e-3)
+        torch.cuda.synchronize()
+        t.check(f"step {step}")
+
+
+def test_adamw_many_launches_equal_one_by_one():
+    """With 32-bit moments and more tensors than a launch takes: adamw_step on each tensor, bit for bit."""
+    t = Many([1 + (64 * i) % 449 for i in range(1100)], "fp32", "bf16", 32, 52)
+    one = [[x.clone() for x in xs] for xs in (t.dp, t.dg, t.dm, t.dv, t.copy)]
+    q.adamw_step_many(t.plan, lr=1e-3, step=4)
+    for p, g, m, v, c in zip(*one):
+        q.adamw_step(p, g, m, v, lr=1e-3, step=4, param_bf16=c)
+    torch.cuda.synchronize()
+    for got, want in zip((t.dp, t.dg, t.dm, t.dv, t.copy), one):
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)

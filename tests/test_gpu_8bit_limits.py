@@ -77,3 +77,78 @@ def test_adamw_many_launches_equal_one_by_one():
     for got, want in zip((t.dp, t.dg, t.dm, t.dv, t.copy), one):
         for x, y in zip(got, want):
             assert torch.equal(x, y)
+
+
+# ---- products ----
+
+SPLIT = [(300, 130, 5000), (130, 258, 6000), (128, 256, 14336)]
+
+
+def split_case(M, N, K, dtype):
+    """A product whose sums go through the workspace, and its exact factors."""
+    assert int(q.lib().ql_fp8_workspace_bytes(M, N, K)) > 0, "the shape is no longer split: take another"
+    rng = np.random.default_rng(M + N + K)
+    a, av = matrix(M, K, "e5m2", rng.standard_normal((M, K)))
+    b, bv = matrix(N, K, "e4m3", rng.standard_normal((N, K)))
+    return dict(a=a, b=b, av=av, bv=bv, out=torch.empty(M, N, dtype=DTYPES[dtype], device=DEV),
+                ws=q.fp8_matmul_workspace(M, N, K, DEV))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_split_products_on_two_streams(dtype):
+    """Products in slices on several streams at once, each with its own workspace, equal the ones run alone."""
+    print(f"split products on streams {dtype}", flush=True)
+    cases = [split_case(*s, dtype) for s in SPLIT]
+    for c in cases:
+        c["want"] = q.fp8_matmul(c["a"], c["b"], dtype=DTYPES[dtype])
+        assert_product(c["want"], c["av"], c["bv"], dtype)
+        c["stream"] = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c in cases:
+            with torch.cuda.stream(c["stream"]):
+                q.fp8_matmul(c["a"], c["b"], out=c["out"], ws=c["ws"])
+    torch.cuda.synchronize()
+    for c in cases:
+        assert torch.equal(c["out"], c["want"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_split_products_captured(dtype):
+    """Products in slices in two captured graphs that share one workspace, replayed in turn with eager products between
+    them and with new operands, equal the eager ones; fp32 ones are added to what is there."""
+    print(f"split products captured {dtype}", flush=True)
+    cases = [split_case(*s, dtype) for s in SPLIT]
+    add = dtype == "fp32"
+    ws = max((c["ws"] for c in cases), key=lambda t: t.numel())
+    run = lambda c, out, ws: q.fp8_matmul(c["a"], c["b"], out=out, accumulate=add, ws=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for c in cases:
+            c["eager"] = torch.zeros_like(c["out"])
+            run(c, c["out"].zero_(), ws)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for part in (cases[:2], cases[1:]):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for c in part:
+                run(c, c["out"], ws)
+    for c in cases:
+        c["out"].zero_()
+        c["eager"].zero_()
+    for rep in range(4):
+        for g, part in zip(graphs, (cases[:2], cases[1:])):
+            for c in part:
+                run(c, c["eager"], c["ws"])
+            g.replay()
+        torch.cuda.synchronize()
+        for c in cases:
+            assert torch.equal(c["out"], c["eager"]), rep
+            if rep == 0 and not add:
+                assert_product(c["out"], c["av"], c["bv"], dtype)
+        if rep == 1:  # new codes reach the captured products
+            for c in cases:
+                c["a"].codes.view(torch.uint8).copy_(c["a"].codes.view(torch.uint8).flip(0))

@@ -105,7 +105,8 @@ size_t ql_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * 16-bit outputs multiply the codes on the 8-bit matrix cores, which add 8
  * consecutive products at a time and drop of each what is below 2^-13 of the
  * largest of them, then add in fp32 (measured on normal data: an error of
- * 1.4e-5 of the result's root mean square, 1/140 of a bf16 rounding).
+ * 1.4e-5 of the result's root mean square, 1/140 of a bf16 rounding).  Where
+ * that is too much, or terms cancel, take fp32 and round it.
  * fp32 outputs multiply the exact values in bf16 (a code times a power of two
  * is a bf16 value) and accumulate in fp32, at half the rate.  Values below
  * 2^-126 may count as 0 there, and values from 2^128 on are infinite.  The

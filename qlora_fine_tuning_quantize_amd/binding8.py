@@ -159,8 +159,8 @@ def fp8_quantize(x: torch.Tensor, block_rows: int = 1, format: torch.dtype = tor
 
     Without out and out_t: returns an FP8Matrix of `format`, or with
     transposed=True that and the transpose.  With out (x) or out_t (x
-    transposed) or both: fills what is given, each in its own format, and
-    returns (out, out_t)."""
+    transposed) or both: fills what is given, each in its own format (`format`
+    is not looked at), and returns (out, out_t)."""
     index = x.get_device()
     if not (x.dim() == 2 and x.is_contiguous() and index >= 0):
         raise ValueError("x is 2-D, contiguous and on the GPU")
@@ -169,6 +169,8 @@ def fp8_quantize(x: torch.Tensor, block_rows: int = 1, format: torch.dtype = tor
     if made:
         out = FP8Matrix.empty(R, C, x.device, format)
         out_t = FP8Matrix.empty(C, R, x.device, format) if transposed else None
+    elif transposed and out_t is None:
+        raise ValueError("transposed with an out given needs an out_t")
     to = to_t = None
     if out is not None:
         to = out._ref

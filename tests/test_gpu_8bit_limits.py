@@ -203,3 +203,15 @@ def test_matmul_own_error(M, N, K, dtype, fmt):
     print(f"  own error {norm(got) / terms:.3e}, cut off {norm(cut) / terms:.3e}", flush=True)
     assert norm(got) <= (1 + 2.0 ** -8) * (norm(cut) + np.sqrt(K / 8) * 2.0 ** -23 * terms)
     assert norm(got) <= 2e-5 * terms
+
+
+# ---- quantisation ----
+
+def test_quantize_transposed_needs_its_output():
+    """A transpose that is asked for is made or refused, never left out."""
+    x = torch.ones(20, 300, device=DEV)
+    m, mt = q.fp8_quantize(x, transposed=True)
+    with pytest.raises(ValueError):
+        q.fp8_quantize(x, out=m, transposed=True)
+    assert q.fp8_quantize(x, out=m, out_t=mt, transposed=True) == (m, mt)
+    assert q.fp8_quantize(x, out_t=mt, transposed=True) == (None, mt)

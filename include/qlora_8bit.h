@@ -165,8 +165,9 @@ typedef struct ql_adamw_tensor {
  * 8-bit moments: a block of 256 consecutive values of a tensor is held as
  * codes and a scale S (value = code * S); the moments' arithmetic is fp32, one
  * rounding for each operation, and a parameter's step is within 2^-21 of
- * itself (eps below 2^-126 counts as that).  With the new moments x of a block
- * and big = max |x|, top = 448 (exp_avg) or 57344 (exp_avg_sq):
+ * itself (eps below 2^-126 counts as that, 2^126 or more as infinite).  With
+ * the new moments x of a block and big = max |x|, top = 448 (exp_avg) or 57344
+ * (exp_avg_sq):
  *     S = big * fp32(1 / top),   t = min(|x| * (top * (1 / big)), top)
  * and t, between the neighbouring codes lo and hi, becomes hi with the
  * probability (t - lo) / (hi - lo), to 16 bits: rounded to the nearest code,
@@ -175,10 +176,14 @@ typedef struct ql_adamw_tensor {
  * of word i % 4 of Philox4x32 (Salmon et al., SC'11) with 7 rounds at counter
  * (i / 4 low word, i / 4 high word, index of the tensor in t, step low word)
  * under the key `seed`, i the element's index.  A value of exp_avg_sq above 0
- * keeps a code above 0, so that no parameter is divided by eps alone.  A
- * block with big < 2^-100 becomes zeros with S = 0; one that holds a NaN or
- * infinity becomes NaN as a whole.  The parameters are updated from the
- * moments before these are rounded to 8 bits.
+ * keeps a code above 0 wherever its block keeps any: a block with big < 2^-100
+ * becomes zeros with S = 0.  Each moment's block is judged by itself, so that of
+ * gradients below 2^-45 or so the second moment can go while the first one
+ * stays, which the next gradient's square and eps alone then divide.  What that
+ * changes is at most 2^-50 / (eps sqrt(1 - beta2^step)) of a step, below 3e-6 at
+ * an eps of 1e-8; under one below 1e-10 such gradients want 32-bit moments.  A
+ * block that holds a NaN or infinity becomes NaN as a whole.  The parameters are
+ * updated from the moments before these are rounded to 8 bits.
  * Scalars are passed by value: a captured step replays its own lr, step and
  * seed, and only grad_scale is read anew; t_device has to outlive the graph.
  * Errors: QL_EINVAL (count < 0, step < 1, null pointers, dtypes, state_bits,

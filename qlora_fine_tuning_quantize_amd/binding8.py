@@ -328,7 +328,8 @@ def adamw_step_many(tensors: AdamWTensors, lr: float, step: int, beta1: float = 
                     grad_scale: torch.Tensor | None = None, seed: int = 0) -> None:
     """One AdamW step in place over all the tensors.  grad_scale: a one-value
     fp32 tensor on the GPU that every gradient is multiplied by first; seed
-    draws the rounding of 8-bit moments."""
+    draws the rounding of 8-bit moments.  (8-bit second moments below 2^-100 are
+    not kept: under an eps below 1e-10, gradients below 3e-14 want 32 bits.)"""
     if tensors.count == 0:
         return
     index = tensors._index

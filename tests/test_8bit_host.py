@@ -285,3 +285,19 @@ def test_reference_rounding_of_moments():
         # mean of n Bernoulli draws: 6 standard deviations, and 2^-16 of the 16-bit draw
         assert abs(rest.mean() - 0.3) < (step[1] - step[0]) * (3 / np.sqrt(rest.size) + 2.0 ** -16) + 1e-7
         assert np.allclose(got.reshape(-1, 256)[:, 0], 1.0, rtol=2.0 ** -22)
+
+
+@pytest.mark.parametrize("eps,step", [(1e-8, 1), (1e-8, 1000), (1e-10, 1), (1e-12, 30)])
+def test_what_dropped_second_moments_change(eps, step):
+    """A block of second moments below 2^-100 is stored as zeros, and one that reaches it keeps all that are above 0;
+    without the dropped ones a step is off by at most 2^-50 / (eps sqrt(1 - beta2^step)) of itself."""
+    rng = np.random.default_rng(8)
+    v = (2.0 ** -rng.uniform(100, 149, 512)).astype(np.float32)
+    v[:256] = np.minimum(v[:256], np.nextafter(np.float32(2.0 ** -100), np.float32(0)))
+    v[3], v[300] = np.nextafter(np.float32(2.0 ** -100), np.float32(0)), np.float32(2.0 ** -100)
+    codes, scale = ref8.store8(v, "e5m2", np.zeros(512, np.int64))
+    assert not codes[:256].any() and scale[0] == 0 and np.all(codes[256:] > 0) and scale[1] > 0
+    correction = np.sqrt(1 - 0.999 ** step)
+    whole = np.sqrt(v[:256].astype(np.float64)) / correction + eps
+    assert np.all(np.abs(1 / eps - 1 / whole) * whole <= 2.0 ** -50 / (eps * correction))
+    assert 2.0 ** -50 / (1e-8 * np.sqrt(1 - 0.999)) < 3e-6

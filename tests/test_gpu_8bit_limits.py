@@ -215,3 +215,86 @@ def test_quantize_transposed_needs_its_output():
         q.fp8_quantize(x, out=m, transposed=True)
     assert q.fp8_quantize(x, out=m, out_t=mt, transposed=True) == (m, mt)
     assert q.fp8_quantize(x, out_t=mt, transposed=True) == (None, mt)
+
+
+# ---- past 2^31 values ----
+
+def test_quantize_large():
+    """2.15e9 values: codes and scales of the last rows, and of the transpose's last columns."""
+    rows, cols = 65541, 32800
+    print("quantize large", flush=True)
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV)
+    for at in range(0, rows, 8192):
+        x[at:at + 8192].normal_()
+    m, mt = q.fp8_quantize(x, transposed=True)
+    alone = q.fp8_quantize(x)
+    torch.cuda.synchronize()
+    first = rows // 128 * 128 - 128  # the last whole block of rows, and what follows
+    tail = f64(host(x[first:]))
+    codes, scales, _ = ref8.quantize(tail, 1, "e4m3")
+    for got in (m, alone):
+        assert np.array_equal(bits8(got.codes[first:]), codes)
+        assert np.array_equal(bits8(got.scales)[:, first:rows], scales[:, :rows - first])
+    codes, scales, _ = ref8.quantize(tail.T, 1, "e4m3")
+    assert np.array_equal(mt.codes.view(torch.uint8)[:, first:].cpu().numpy(), codes)
+    assert np.array_equal(bits8(mt.scales)[first // 128:], scales)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_matmul_large(dtype):
+    """A matrix of 2.15e9 codes against few rows and as few rows: outputs at its end.  And an output of 2.2e9 values."""
+    print(f"matmul large {dtype}", flush=True)
+    rows, K = 65541, 32800
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device=DEV)
+    for at in range(0, rows, 8192):
+        x[at:at + 8192].normal_()
+    a = q.fp8_quantize(x)
+    tail = f64(host(x[-150:]))
+    del x
+    av = ref8.dequantize(*ref8.quantize(tail, 1, "e4m3")[:2], 150, "e4m3")[:, :K]
+    rng = np.random.default_rng(3)
+    for n in (5, 70):
+        b, bv = matrix(n, K, "e4m3", rng.standard_normal((n, K)))
+        assert_product(q.fp8_matmul(a, b, dtype=DTYPES[dtype])[-150:], av, bv, dtype, what=f"many rows x {n}")
+        assert_product(q.fp8_matmul(b, a, dtype=DTYPES[dtype])[:, -150:], bv, av, dtype, what=f"{n} x many rows")
+    del a
+    M, N, K = 47000, 47001, 40
+    a, b = (q.fp8_quantize(torch.randn(s, K, device=DEV)) for s in (M, N))
+    out = q.fp8_matmul(a, b, dtype=DTYPES[dtype])
+    av, bv = (ref8.dequantize(bits8(m.codes[-100:]), bits8(m.scales)[:, s - 100:s], 100, "e4m3")[:, :K]
+              for m, s in ((a, M), (b, N)))
+    assert_product(out[-100:, -100:], av, bv, dtype, what="many outputs")
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_many_large(bits):
+    """A tensor of 2^31 + 1501 values beside small ones: its end, and the ones after it."""
+    print(f"adamw_many large {bits}", flush=True)
+    n = 2 ** 31 + 1501
+    base = n // 256 * 256 - 4096  # the last values are checked, from a block's border on
+    p = [torch.empty(k, device=DEV).normal_() for k in (300, n, 700)]
+    g = [torch.empty(k, dtype=torch.bfloat16, device=DEV).normal_() for k in (300, n, 700)]
+    plan = q.AdamWTensors.zeros(p, g, bits)
+    before = [t[base if t.numel() == n else 0:].cpu().numpy() for t in p]
+    q.adamw_step_many(plan, lr=2e-3, step=1, seed=12)
+    torch.cuda.synchronize()
+    for i, k in enumerate((300, n, 700)):
+        at = base if k == n else 0
+        gv = f64(host(g[i][at:])).astype(np.float32)
+        zero = np.zeros(len(gv), np.float32)
+        want, m, v = ref8.adamw(before[i], gv, zero, zero, lr=2e-3, step=1)
+        got = p[i][at:].cpu().numpy()
+        if bits == 32:
+            assert np.array_equal(got, want), i
+            assert np.array_equal(plan.exp_avgs[i][at:].cpu().numpy(), m), i
+            assert np.array_equal(plan.exp_avg_sqs[i][at:].cpu().numpy(), v), i
+            continue
+        # the bound of Many.check
+        moved = np.abs(want.astype(np.float64) - before[i] * (1 - 2e-3 * 0.01))
+        assert np.all(np.abs(got.astype(np.float64) - want) <= 2.0 ** -21 * moved + 4 * 2.0 ** -24 * np.abs(want)), i
+        words = np.stack(ref8.philox(np.arange(at // 4, -(-k // 4)), i, 1, 12), 1).reshape(-1)[:k - at].astype(np.int64)
+        for codes, scale, x, fmt, r in ((plan.exp_avgs, plan.exp_avg_scales, m, "e4m3", words & 0xFFFF),
+                                        (plan.exp_avg_sqs, plan.exp_avg_sq_scales, v, "e5m2", words >> 16)):
+            c, s = ref8.store8(x, fmt, r)
+            assert np.array_equal(bits8(codes[i][at:]), c), (i, fmt)
+            assert np.array_equal(scale[i][at // 256:].cpu().numpy(), s[:-(-len(x) // 256)]), (i, fmt)

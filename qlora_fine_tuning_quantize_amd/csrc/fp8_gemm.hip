@@ -15,10 +15,11 @@
 //     waits for the load unit starves the matrix core: in the first quarter of
 //     a half block 761 us, in all of it 710;
 //   rows of LDS freed and loaded again in halves, so that loads go on all the
-//     time and have two blocks' time to arrive: 660 us, 2.9 PFLOP/s, matrix cores
-//     busy 82 % of the time at the clock that their power leaves (on registers
-//     alone 3.6 - 4.1 PFLOP/s with such operands).
-// Where 256 x 256 tiles leave CUs idle: 128 x 256 (2.4 PFLOP/s: LDS, with 1152 of
+//     time and have two blocks' time to arrive: 660 us.
+// (Best of five runs each, as they were built.)  In a long run it takes 690 to
+// 707 us, 2.75 PFLOP/s, matrix cores busy 83 % of the time at the clock that
+// their power leaves (on registers alone 3.6 - 4.1 PFLOP/s with such operands).
+// Where 256 x 256 tiles leave CUs idle: 128 x 256 (2.3 PFLOP/s: LDS, with 1152 of
 // 1024 cycles, bounds it), then 128 x 128, and slices of K.
 //
 // fp32 outputs: every 8-bit matrix instruction adds with fewer bits than fp32
@@ -497,8 +498,8 @@ __global__ __launch_bounds__(256, 1) void k_fp8_gemm(Fp8In a, Fp8In b,
 // the tiles, 14336 x 4096 x 2000 took 265 us, so 257).  Two workgroups to a CU, so
 // that one multiplies while the other writes: with tiles of 256 x 256, fewer
 // conversions and one workgroup, it took 346 us instead of 233.  Bound by both at
-// once: vector instructions 70 % of the time, matrix cores 63 %; long products
-// come to 1.37 PFLOP/s.
+// once: vector instructions 70 % of the time, matrix cores 61 %; long products
+// come to 1.29 PFLOP/s (4096 x 4096 x 16384).
 template <int TM, int TN, bool A_E5M2, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void k_fp8_gemm_f32(Fp8In a, Fp8In b,
                                                          float *__restrict__ out, bool accumulate,

@@ -229,8 +229,10 @@ class AdamWTensors:
     that is written; the object keeps them alive.  Gradients are read from the
     tensors given here: write new ones into them.  Their addresses are uploaded
     once, here, and their memory is kept: a tensor that is given other memory
-    (p.data = ...) needs a new object.  A graph that captures a step needs the
-    object as long as it lives."""
+    (p.data = ...) needs a new object.  Memory made here (the addresses, and the
+    moments of zeros()) may go with the object while a step on another stream
+    still runs; of tensors given, that is their owner's care.  A graph that
+    captures a step needs the object as long as it lives."""
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None,
                  exp_avg_sq_scales=None, copies=None):
@@ -283,7 +285,9 @@ class AdamWTensors:
         self._grad_code, self._copy_code = _code(grad_type), _code(copy_type)
         self._refs = (self._structs.data_ptr(), self._table.data_ptr()) if n else (None, None)
         self._index = index
-        self._stream = _raw_stream(index) if n else None
+        # memory made here, and the streams that it is known to be used on
+        self._own = [self._table] if n else []
+        self._streams = {_raw_stream(index)} if n else set()
 
     @staticmethod
     def _no_overlap(spans):
@@ -308,11 +312,14 @@ class AdamWTensors:
                                        device=p.device).view(dt)
         sc = lambda p: torch.zeros(-(-p.numel() // STATE_BLOCK), device=p.device)
         if bits == 32:
-            return AdamWTensors(params, grads, [mk(p, torch.float32) for p in params],
-                                [mk(p, torch.float32) for p in params], copies=copies)
-        return AdamWTensors(params, grads, [mk(p, torch.float8_e4m3fn) for p in params],
-                            [mk(p, torch.float8_e5m2) for p in params], [sc(p) for p in params],
-                            [sc(p) for p in params], copies)
+            made = [[mk(p, torch.float32) for p in params] for _ in range(2)]
+        else:
+            made = [[mk(p, torch.float8_e4m3fn) for p in params],
+                    [mk(p, torch.float8_e5m2) for p in params],
+                    [sc(p) for p in params], [sc(p) for p in params]]
+        plan = AdamWTensors(params, grads, *made, copies=copies)
+        plan._own += [t.detach() for given in made for t in given]
+        return plan
 
     params = property(lambda self: self._tensors[0])
     grads = property(lambda self: self._tensors[1])
@@ -337,9 +344,12 @@ def adamw_step_many(tensors: AdamWTensors, lr: float, step: int, beta1: float = 
                                        and grad_scale.numel() == 1
                                        and grad_scale.get_device() == index):
         raise ValueError("grad_scale is one fp32 value on the parameters' GPU")
-    if _raw_stream(index) != tensors._stream:
-        # the table's memory is not to be given away before this stream has read it
-        tensors._table.record_stream(torch.cuda.current_stream(index))
+    if _raw_stream(index) not in tensors._streams:
+        # memory made for the object is not to be given away before this stream is done with it
+        stream = torch.cuda.current_stream(index)
+        for t in tensors._own:
+            t.record_stream(stream)
+        tensors._streams.add(stream.cuda_stream)
     _call(lib8().ql_adamw_step_many, "ql_adamw_step_many", index, tensors.count, *tensors._refs,
           tensors._grad_code, tensors._state_bits, tensors._copy_code,
           None if grad_scale is None else grad_scale.data_ptr(), lr, beta1, beta2, eps,

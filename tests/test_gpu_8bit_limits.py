@@ -298,3 +298,33 @@ def test_adamw_many_large(bits):
             c, s = ref8.store8(x, fmt, r)
             assert np.array_equal(bits8(codes[i][at:]), c), (i, fmt)
             assert np.array_equal(scale[i][at // 256:].cpu().numpy(), s[:-(-len(x) // 256)]), (i, fmt)
+
+
+# ---- streams and graphs ----
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_moments_made_here_on_another_stream(bits):
+    """A step on another stream, whose object, and with it the moments that zeros() made, is dropped right after the
+    call: what takes their memory next neither changes the step nor is written by it."""
+    print(f"adamw moments made here {bits}", flush=True)
+    gen = torch.Generator(device=DEV).manual_seed(61)
+    sizes = [70000, 300, 128 * 1024]
+    p, g = ([torch.randn(n, generator=gen, device=DEV) for n in sizes] for _ in range(2))
+    want = [x.clone() for x in p]
+    plain, dropped = q.AdamWTensors.zeros(want, g, bits), q.AdamWTensors.zeros(p, g, bits)
+    for plan in (plain, dropped):
+        q.adamw_step_many(plan, lr=1e-2, step=1, seed=3)
+    q.adamw_step_many(plain, lr=1e-2, step=2, seed=4)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(2000000)
+        q.adamw_step_many(dropped, lr=1e-2, step=2, seed=4)
+        del dropped, plan
+    scribble = [torch.full((n * (4 if bits == 32 else 1),), 0x77, dtype=torch.uint8, device=DEV) for n in sizes * 2]
+    scribble += [torch.full((-(-n // 256),), 1e9, device=DEV) for n in sizes * 2]
+    stream.synchronize()
+    torch.cuda.synchronize()
+    for x, y in zip(p, want):
+        assert torch.equal(x, y)
+    assert all(bool((x == (0x77 if x.dtype == torch.uint8 else 1e9)).all()) for x in scribble)

@@ -328,3 +328,30 @@ def test_adamw_moments_made_here_on_another_stream(bits):
     for x, y in zip(p, want):
         assert torch.equal(x, y)
     assert all(bool((x == (0x77 if x.dtype == torch.uint8 else 1e9)).all()) for x in scribble)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_launches_captured(bits):
+    """A captured step of more tensors than a launch takes, replayed with eager steps of another object between the
+    replays, gives what they give; only the gradients and their factor are read anew."""
+    print(f"adamw launches captured {bits}", flush=True)
+    sizes = [(53 * i) % 700 for i in range(1100)]
+    a, b = Many(sizes, "bf16", "bf16", bits, 71), Many(sizes, "bf16", "bf16", bits, 71)
+    scale = torch.full((1,), 0.5, device=DEV)
+    step = lambda t: q.adamw_step_many(t.plan, lr=1e-3, step=7, grad_scale=scale, seed=8)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(a)
+    for rep in range(3):
+        step(b)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in ("dp", "dm", "dv", "copy") + (("dms", "dvs") if bits == 8 else ()):
+            for x, y in zip(getattr(a, name), getattr(b, name)):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), (rep, name)
+        scale.fill_(0.25)
+        for x, y in zip(a.dg, b.dg):
+            x.neg_()
+            y.neg_()

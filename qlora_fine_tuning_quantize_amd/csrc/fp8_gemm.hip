@@ -16,8 +16,8 @@
 //     a half block 761 us, in all of it 710;
 //   rows of LDS freed and loaded again in halves, so that loads go on all the
 //     time and have two blocks' time to arrive: 660 us.
-// (Best of five runs each, as they were built.)  In a long run it takes 690 to
-// 707 us, 2.75 PFLOP/s, matrix cores busy 83 % of the time at the clock that
+// (Best of five runs each, as they were built.)  In a long run it takes 682 to
+// 707 us, 2.7 - 2.8 PFLOP/s, matrix cores busy 83 % of the time at the clock that
 // their power leaves (on registers alone 3.6 - 4.1 PFLOP/s with such operands).
 // Where 256 x 256 tiles leave CUs idle: 128 x 256 (2.3 PFLOP/s: LDS, with 1152 of
 // 1024 cycles, bounds it), then 128 x 128, and slices of K.
